@@ -692,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           last = __shfl_sync(0xffffffffu, before, 0) == (uint32_t)(p1 - p0);
         }
         if (last) {
+          __syncwarp();                          // lane 0's acquire comes before the other lanes' loads (a shuffle orders no memory)
           if (lane == 0) *counter = 0;
           // m and l of the parts, MB at a time, then O in blocks of CB 16-byte
           // chunks (the loads of a block are in flight together), in the

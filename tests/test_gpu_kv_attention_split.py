@@ -1,0 +1,31 @@
+"""Units of the NVFP4 attention that several CTAs share: the plans that cut
+them, the joins of their partial results, and waits that give up."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_kv_attention import Problem
+
+pytestmark = pytest.mark.gpu
+
+
+def _equal(a, b):
+    return torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("seqs,hq,hkv,d", [
+    ([(2600, 300)], 10, 2, 128), ([(1500, 300), (4000, 1), (900, 33)], 8, 2, 64), ([(9000, 40)], 8, 1, 128),
+    ([(6000, 70)], 8, 1, 64), ([(5000, 4)] * 3, 16, 2, 128)])
+def test_joins_take_this_calls_partial_results(lib, seqs, hq, hkv, d):
+    """Two calls of one shape and different data take turns on one workspace:
+    a partial result of the call before, read too early, would show."""
+    ps = [Problem(seqs, hq, hkv, d, 16, seed=s, q_scale=q) for s, q in ((11, 1.0), (12, 5.0))]
+    ts = [p.device() for p in ps]
+    alone = [p.call(lib, t, p.workspace(lib)) for p, t in zip(ps, ts)]
+    torch.cuda.synchronize()
+    assert not _equal(*alone)
+    ws = ps[0].workspace(lib)
+    got = [(i, ps[i].call(lib, ts[i], ws)) for i in [0, 1] * 20]
+    torch.cuda.synchronize()
+    assert all(_equal(o, alone[i]) for i, o in got)
+    assert not ws[:65536].any()
