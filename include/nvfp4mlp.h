@@ -518,6 +518,8 @@ nvfp4_status nvfp4_kv_cache_read(const uint8_t *cache, const int64_t *slots, con
  *   block_table  int32 [batch, max_pages] DEVICE: the pages of each sequence
  *                in order; entries past a sequence's length are not used.  The
  *                tokens of an entry outside [0, pages) are not attended to.
+ *                With a window, pages in front of every query's may have been
+ *                given away: what they hold does not reach the result.
  *   seq_lens     int32 [batch] DEVICE: cached tokens of each sequence, its
  *                queries included (clamped to max_pages * page_size)
  *   qk_scale     fp32 [1]: softmax scale / gs of the keys

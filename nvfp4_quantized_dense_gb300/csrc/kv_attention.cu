@@ -288,10 +288,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NQ>::CTAS)
     const int row0 = tile * ROWS, rows = min(sq.qn * group - row0, ROWS);
     const int first = sq.pos0 + div_small(row0, inv_group), last = sq.pos0 + div_small(row0 + rows - 1, inv_group);   // positions
     const int win = (int)a.window;
+    const int seen = win > 0 ? max(first - win + 1, 0) : 0;      // first token that any row of the tile sees
     // the segment's steps that any row of the tile sees
     int st0 = sq.lo_step + step_at(pos), st1 = sq.lo_step + step_at(seg1);
     st1 = min(st1, last < 0 ? 0 : last / kStep + 1);
-    if (win > 0) st0 = max(st0, max(first - win + 1, 0) / kStep);
+    st0 = max(st0, seen / kStep);
 
     // ---- the warp's steps: st0 + warp, + kWarps, ...  Lanes 2i, 2i+1 look up the
     // pages of the two records of step number base + i; `next` runs 16 steps ahead.
@@ -509,9 +510,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NQ>::CTAS)
             w[i][0] = *reinterpret_cast<const uint32_t *>(rp + R::V_CODES + ((g >> 1) * kKvGroup + 4 * c + i) * 8 + (g & 1) * 4);
           vsf = *reinterpret_cast<const uint32_t *>(rp + R::V_SF + (g >> 1) * kKvGroup + 4 * c);
         }
-        if (masked) {                             // scales past the end may be NaN: their tokens count 0
-          const int left = ((valid >> rec) & 1) ? sq.len - (t0 + rec * kKvGroup + 4 * c) : 0;
-          vsf = left >= 4 ? vsf : left <= 0 ? 0u : vsf & ((1u << (8 * left)) - 1u);
+        if (masked) {                             // past the end, and in front of every row's window
+          const int at = t0 + rec * kKvGroup + 4 * c;
+          vsf = scales_within(vsf, seen - at, ((valid >> rec) & 1) ? sq.len - at : 0);
         }
         const uint32_t s01 = e4m3x2_to_f16x2(vsf & 0xffffu), s23 = e4m3x2_to_f16x2(vsf >> 16);
 #pragma unroll

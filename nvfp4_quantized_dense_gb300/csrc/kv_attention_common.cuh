@@ -16,6 +16,14 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2^-22 relative; 2^-in
   return r;
 }
 
+// The E4M3 scales of four tokens in a row with those outside [from, to) zeroed
+// (places counted from the first of the four): the bytes of a token that no
+// query sees may be anything, NaN too, and 0 times NaN would reach every row.
+__device__ __forceinline__ uint32_t scales_within(uint32_t four, int from, int to) {
+  four = to >= 4 ? four : to <= 0 ? 0u : four & ((1u << (8 * to)) - 1u);
+  return from <= 0 ? four : from >= 4 ? 0u : four & (~0u << (8 * from));
+}
+
 // The line [0, total) in `parts` equal pieces, the first total % parts of them
 // one longer.
 struct Line {

@@ -132,6 +132,7 @@ struct Segment {
   int b, len, head, rows;
   int token, pos, rem; // of its first row: token, position, query head of the group
   int first, count;
+  int seen;            // first token that any row of the unit sees
   int whole;           // the whole unit
   int p0, p1;          // else: the parts that share it
 };
@@ -890,14 +891,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (v_on) {
-          // tokens past the end count 0, whatever their scales hold
-          const int left = v_there ? w.len - ((w.first + j) * kTile + 8 * v_oct) : 0;
-          uint32_t sf[2] = {vsf.x, vsf.y};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int x = left - 4 * i;
-            sf[i] = x >= 4 ? sf[i] : x <= 0 ? 0u : sf[i] & ((1u << (8 * x)) - 1u);
-          }
+          // tokens past the end and in front of every row's window count 0, whatever their scales hold
+          const int at = (w.first + j) * kTile + 8 * v_oct, to = v_there ? w.len - at : 0, from = w.seen - at;
+          const uint32_t sf[2] = {scales_within(vsf.x, from, to), scales_within(vsf.y, from - 4, to - 4)};
           uint32_t s2[4];
 #pragma unroll
           for (int p = 0; p < 4; ++p) s2[p] = e4m3x2_to_f16x2((sf[p >> 1] >> (16 * (p & 1))) & 0xffffu);
@@ -1031,6 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int k = w.u.tile * kRows / group;
           g.b = w.u.b, g.len = w.u.len, g.head = w.head, g.rows = w.rows(), g.first = w.first, g.count = w.count;
           g.token = w.u.q0 + k, g.pos = w.u.pos0 + k, g.rem = w.u.tile * kRows - k * group;
+          g.seen = a.window > 0 ? max(g.pos - (int)a.window + 1, 0) : 0;
           g.whole = w.whole;
           if (!w.whole) {
             g.p0 = line.part_of(w.unit0);
