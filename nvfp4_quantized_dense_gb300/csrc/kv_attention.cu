@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NQ>::CTAS)
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // exponent field of the magnitude -> 2^(141 - e); subnormal and zero rows as the smallest normal one
       const int e = min(max((int)(top >> 7), 15), 254);
-      const float up = copysignf(__uint_as_float((uint32_t)(127 + 141 - e) << 23), qk0);   // 2^126 .. 2^-113
+      const float up = row_factor((uint32_t)(127 + 141 - e), qk0);       // 2^126 .. 2^-113
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) qf[n][i] = f16x2(bf16_lo(qf[n][i]) * up, bf16_hi(qf[n][i]) * up);
       if constexpr (C::Q_BYTES > 0)

@@ -16,6 +16,13 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2^-22 relative; 2^-in
   return r;
 }
 
+// What a query row is multiplied by: the power of two with exponent field e,
+// with the sign of the scores' scale, or that scale itself where it is a NaN:
+// the scores that a row sees are NaN then, and the masked ones still -inf.
+__device__ __forceinline__ float row_factor(uint32_t e, float qk) {
+  return qk == qk ? copysignf(__uint_as_float(e << 23), qk) : qk;
+}
+
 // The E4M3 scales of four tokens in a row with those outside [from, to) zeroed
 // (places counted from the first of the four): the bytes of a token that no
 // query sees may be anything, NaN too, and 0 times NaN would reach every row.

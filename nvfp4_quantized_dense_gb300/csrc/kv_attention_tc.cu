@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int o = (i0 + i) * RPI + lane / CPR, e = min(max((int)(max(top[i] & 0xffffu, top[i] >> 16) >> 7), 15), 254);
-            const float up = copysignf(__uint_as_float((uint32_t)(268 - e) << 23), qk0);
+            const float up = row_factor((uint32_t)(268 - e), qk0);
             const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
             const __nv_bfloat162 up2 = __float2bfloat162_rn(up);
             uint32_t y[4];

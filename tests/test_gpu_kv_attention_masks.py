@@ -1,9 +1,10 @@
-"""What the NVFP4 attention must not use: tokens in front of a window."""
+"""What the NVFP4 attention must not use (tokens in front of a window), and
+scale factors that are not numbers."""
 import numpy as np
 import pytest
 import torch
 
-from gpu_util import dev
+from gpu_util import dev, scalar
 from kv_util import offsets
 from test_gpu_kv_attention import Problem
 
@@ -59,3 +60,27 @@ def test_stale_bytes_in_front_of_a_window(lib, seqs, hq, hkv, page, window, d):
             torch.cuda.synchronize()
             assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
 
+
+SCALES = [([(40, 1), (300, 1), (0, 1)], 8, 2), ([(300, 4), (2, 4)], 8, 1), ([(300, 40), (20, 30)], 8, 2)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("seqs,hq,hkv", SCALES)
+def test_scales_that_are_nan(lib, seqs, hq, hkv, d):
+    """A NaN score scale makes every row NaN that sees anything, log-sum-exp
+    included; a NaN value scale the outputs alone."""
+    p = Problem(seqs, hq, hkv, d, 16, seed=22)
+    t, ws = p.device(), p.workspace(lib)
+    ref = p.call(lib, t, ws)
+    torch.cuda.synchronize()
+    sees = torch.isfinite(ref[1])
+    assert not sees.all() and sees.any()
+    for sign in (1.0, -1.0):
+        out, lse = p.call(lib, dict(t, qk=scalar(sign * float("nan"))), ws)
+        torch.cuda.synchronize()
+        assert torch.isnan(out[sees]).all() and torch.isnan(lse[sees]).all()
+        assert (out[~sees] == 0).all() and torch.isneginf(lse[~sees]).all()
+    out, lse = p.call(lib, dict(t, vs=scalar(float("nan"))), ws)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[sees]).all() and (out[~sees] == 0).all()
+    assert torch.equal(lse, ref[1])
