@@ -382,6 +382,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NQ>::CTAS)
       l[n][0] = l[n][1] = 0.0f;
     }
 
+    // (the copies may be there before the first poll, or while it sleeps in the
+    // barrier unit: a limit of 1 gives up without one)
+    if (issued > 0 && a.wait_limit == 1) gave_up = true;
     int done = 0;
     for (; done < count && !gave_up; ++done) {
       if (!ptx::mbar_wait_bounded(&full[get], phase, a.wait_limit, kTimeoutNs, &s_abort[warp])) gave_up = true;

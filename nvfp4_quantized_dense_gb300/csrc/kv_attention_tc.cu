@@ -975,6 +975,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           issue_s(t, n);
           if (t == nt - 1) commit(&s_kempty[n & 1]);
         }
+        // (what is waited for comes while a poll sleeps: with a limit of 1 the
+        // first probabilities' wait gives up without one, S in flight, and the
+        // other roles' by it)
+        if (limit == 1) ok = false;
         for (int j = 0; j < count && ok; ++j, ++n) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {

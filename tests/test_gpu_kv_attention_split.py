@@ -29,3 +29,30 @@ def test_joins_take_this_calls_partial_results(lib, seqs, hq, hkv, d):
     torch.cuda.synchronize()
     assert all(_equal(o, alone[i]) for i, o in got)
     assert not ws[:65536].any()
+
+
+# What gives up first: the decode form's wait for its copies, the chunk form's
+# for the first probabilities.
+GIVES_UP = [([(9000, 1)] * 4, 8, 2, 128), ([(9000, 4)] * 2, 16, 2, 64), ([(2600, 700)], 8, 2, 128), ([(2600, 70)], 8, 2, 64)]
+
+
+@pytest.mark.parametrize("seqs,hq,hkv,d", GIVES_UP)
+def test_a_wait_that_runs_out_is_reported(lib, seqs, hq, hkv, d):
+    """With a wait limit of one poll both forms record the timeout and return;
+    after the workspace is zero-filled again the next call is right."""
+    p = Problem(seqs, hq, hkv, d, 16, seed=13)
+    t = p.device()
+    ref = p.call(lib, t, p.workspace(lib))
+    assert lib.nvfp4_get_device_status() == lib.OK
+    ws = p.workspace(lib)
+    lib.nvfp4_set_wait_limit(1)
+    try:
+        p.call(lib, t, ws)
+        status = lib.nvfp4_get_device_status()
+    finally:
+        lib.nvfp4_set_wait_limit(0)
+    assert status == lib.ERR_DEVICE_TIMEOUT
+    ws.zero_()
+    again = p.call(lib, t, ws)
+    torch.cuda.synchronize()
+    assert _equal(again, ref) and lib.nvfp4_get_device_status() == lib.OK
