@@ -692,9 +692,10 @@ cudaError_t launch(const KvAttentionParams &a, cudaStream_t st) {
   const double fit = 2147483647.0 / line;
   if (fit < 1.0) return cudaErrorInvalidValue;
   const int64_t slice = fit < (double)a.batch ? (int64_t)fit : a.batch;
-  int64_t room = a.ws_bytes > kCounterArea ? (int64_t)((a.ws_bytes - kCounterArea) / part_bytes<D, NQ>()) : 0;
-  if (room > kCounterSlots) room = kCounterSlots;
-  const bool split = room > 0;
+  // With less than the room asked for no unit is split, on all CTAs: as many
+  // CTAs as there is room for may be one.
+  const int64_t room = a.ws_bytes > kCounterArea ? (int64_t)((a.ws_bytes - kCounterArea) / part_bytes<D, NQ>()) : 0;
+  const bool split = room >= kSmsPlanned * C::CTAS;
   for (int64_t b0 = 0; b0 < a.batch; b0 += slice) {
     const KvAttentionParams p = kv_attention_slice(a, b0, slice);
     int64_t most = (int64_t)num_sms() * C::CTAS;

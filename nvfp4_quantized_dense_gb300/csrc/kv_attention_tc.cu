@@ -1061,7 +1061,7 @@ cudaError_t launch_tc_attention(const KvAttentionParams &a, cudaStream_t st) {
     return e;
   const int64_t part_bytes = 2 * (int64_t)C::PART_FLOATS * 4;
   const int64_t room = a.ws_bytes > kCounterArea ? (int64_t)(a.ws_bytes - kCounterArea) / part_bytes : 0;
-  const bool split = room > 0;
+  const bool split = room >= kSmsPlanned;        // (with less than the room asked for no unit is split, on all CTAs)
   // A launch takes up to kMaxBatch sequences, and a line of 31 bits: larger batches go in slices.
   const int64_t rows = a.max_q * (a.q_heads / a.kv_heads);
   const double line = (double)a.kv_heads * (double)((rows + kRows - 1) / kRows) *

@@ -56,3 +56,22 @@ def test_a_wait_that_runs_out_is_reported(lib, seqs, hq, hkv, d):
     again = p.call(lib, t, ws)
     torch.cuda.synchronize()
     assert _equal(again, ref) and lib.nvfp4_get_device_status() == lib.OK
+
+
+@pytest.mark.parametrize("seqs,hq,hkv,d", [([(4100, 1), (2050, 1)], 8, 1, 128), ([(5000, 4)] * 2, 8, 1, 64),
+                                           ([(2600, 300)], 8, 2, 128)])
+def test_a_workspace_that_is_too_small_splits_nothing(lib, seqs, hq, hkv, d):
+    """Room for a few partial results is not room for the call's: units stay
+    whole, as without a workspace, and every CTA works."""
+    p = Problem(seqs, hq, hkv, d, 16, seed=14)
+    t = p.device()
+    whole = p.call(lib, t, None)
+    full = p.workspace(lib)
+    split = p.call(lib, t, full)
+    torch.cuda.synchronize()
+    assert not _equal(whole, split)
+    for n in (65536 // 2, 65536 + (full.numel() - 65536) // 40, full.numel() - 16):
+        ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        got = p.call(lib, t, ws)
+        torch.cuda.synchronize()
+        assert _equal(got, whole) and not ws.any()
