@@ -535,8 +535,10 @@ nvfp4_status nvfp4_kv_cache_read(const uint8_t *cache, const int64_t *slots, con
  * Scores, softmax statistics and sums are fp32; keys and values enter the
  * products exactly, probabilities as f16.  Requires q_heads % kv_heads == 0,
  * q_heads <= 1024, batch <= 65536, tokens < 2^31 / q_heads, max_q <= 2^28,
- * max_pages * page_size <= 2^30 and kv_heads * (max_q * q_heads / kv_heads / 8
- * + 1) * (max_pages * page_size + 256) < 2^35. */
+ * T = max_pages * page_size <= 2^30 and, with rows = max_q * q_heads /
+ * kv_heads, below 2^31 both of kv_heads * ceil(rows / 32) * (T / 32 + 13) for
+ * up to 32 rows (64 at head_dim 64) and kv_heads * ceil(rows / 256) * (T / 128
+ * + 5) for more: a chunk of 131,072 tokens of 64 heads on 8 is far inside. */
 nvfp4_status nvfp4_kv_attention(const uint16_t *q, int64_t q_stride, const int32_t *cu_q, const uint8_t *cache,
                                 const int32_t *block_table, const int32_t *seq_lens, const float *qk_scale,
                                 const float *v_scale, uint16_t *out, float *lse, int64_t tokens, int64_t batch,

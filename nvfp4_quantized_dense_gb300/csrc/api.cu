@@ -607,9 +607,8 @@ nvfp4_status nvfp4_kv_attention(const uint16_t *q, int64_t q_stride, const int32
       max_pages > (int64_t(1) << 30) || max_pages * page_size > (int64_t(1) << 30) ||
       window >= (int64_t(1) << 31) || bad_rows(q_stride, q_heads, head_dim))
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
-  // the length of one sequence's share of the work is counted in 31 bits
-  if ((double)kv_heads * (double)(max_q * (q_heads / kv_heads) / 8 + 1) * (double)(max_pages * page_size + 256) >=
-      34359738368.0)
+  // a sequence's share of the work is counted in 31 bits
+  if (kv_attention_places(max_q, q_heads, kv_heads, head_dim, max_pages * page_size) > 2147483647.0)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (!cu_q && tokens != batch * max_q) return NVFP4_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || (workspace && !aligned16(workspace)))

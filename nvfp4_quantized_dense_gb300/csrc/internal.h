@@ -208,11 +208,16 @@ struct KvAttentionParams {
 };
 size_t kv_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads,
                                     int64_t head_dim);
+// Places of one sequence on the line of work that the form for these sizes
+// cuts, at most; the kernels count a launch's in 31 bits.  tokens: the block
+// table's capacity.
+double kv_attention_places(int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t tokens);
 cudaError_t launch_kv_attention(const KvAttentionParams &a, cudaStream_t st);
 // The same call for sequences b0 .. b0 + n - 1 of the batch.
 KvAttentionParams kv_attention_slice(const KvAttentionParams &a, int64_t b0, int64_t n);
 // Its prefill-sized form (kv_attention_tc.cu).
 size_t kv_attention_tc_workspace_bytes(int64_t head_dim);
+double kv_attention_tc_places(int64_t rows, int64_t kv_heads, int64_t tokens);
 cudaError_t launch_kv_attention_tc(const KvAttentionParams &a, cudaStream_t st);
 
 }  // namespace nvfp4

@@ -84,13 +84,16 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kDrainPolls = 1u << 22;
 constexpr int kSmsPlanned = 152;             // workspace sizing (the launch takes what fits)
 
+// What a unit's beginning and end cost, in steps, by its groups of 8 rows.
+constexpr int unit_cost(int groups) { return groups == 1 ? 8 : 12; }
+
 template <int D, int NQ>
 struct Cfg {
   using R = KvRecord<D>;
   static constexpr int ROWS = 8 * NQ;                       // query rows of a tile
   static constexpr int CTAS = (NQ == 1 ? 4 : NQ == 2 ? 3 : 2) + (D == 64 && NQ == 2);    // per SM, by registers
   static constexpr int STAGES = NQ == 1 ? 2 : 3;
-  static constexpr int UNIT_COST = NQ == 1 ? 8 : 12;        // what a unit's beginning and end cost, in steps
+  static constexpr int UNIT_COST = unit_cost(NQ);
   static constexpr int STAGE_BYTES = 2 * R::BYTES;
   static constexpr int RING_BYTES = kWarps * STAGES * STAGE_BYTES;
   static constexpr int JOIN_BYTES = kWarps * ROWS * (D + 2) * 4;
@@ -685,12 +688,9 @@ cudaError_t launch(const KvAttentionParams &a, cudaStream_t st) {
           [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); }))
     return e;
   // The kernel counts steps in 31 bits: a batch whose line could be longer is taken in slices.
-  const int64_t rows = a.max_q * (a.q_heads / a.kv_heads);
-  const int64_t steps = (a.max_pages * a.page_size + kStep - 1) / kStep;
-  const int64_t tiles = (rows + C::ROWS - 1) / C::ROWS;
-  const double line = (double)a.kv_heads * (double)tiles * (double)(steps + C::UNIT_COST);     // of one sequence, at most
+  const double line = kv_attention_places(a.max_q, a.q_heads, a.kv_heads, a.head_dim, a.max_pages * a.page_size);
   const double fit = 2147483647.0 / line;
-  if (fit < 1.0) return cudaErrorInvalidValue;
+  if (fit < 1.0) return cudaErrorInvalidValue;               // (the entry point has seen to that)
   const int64_t slice = fit < (double)a.batch ? (int64_t)fit : a.batch;
   // With less than the room asked for no unit is split, on all CTAs: as many
   // CTAs as there is room for may be one.
@@ -740,6 +740,13 @@ static int64_t tc_rows(int64_t head_dim) { return head_dim == 128 ? 32 : 64; }
 static int tile_groups(int64_t rows) {
   const int64_t tiles = (rows + 31) / 32;
   return (int)((rows + 8 * tiles - 1) / (8 * tiles));
+}
+
+// One sequence's places on the line at most, as either form counts them.
+double kv_attention_places(int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t tokens) {
+  const int64_t rows = max_q * (q_heads / kv_heads);
+  if (rows > tc_rows(head_dim)) return kv_attention_tc_places(rows, kv_heads, tokens);
+  return (double)kv_heads * (double)((rows + 31) / 32) * (double)((tokens + kStep - 1) / kStep + unit_cost(tile_groups(rows)));
 }
 
 size_t kv_attention_workspace_bytes(int64_t, int64_t, int64_t max_q, int64_t q_heads, int64_t kv_heads,

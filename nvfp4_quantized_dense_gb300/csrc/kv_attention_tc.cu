@@ -1063,11 +1063,9 @@ cudaError_t launch_tc_attention(const KvAttentionParams &a, cudaStream_t st) {
   const int64_t room = a.ws_bytes > kCounterArea ? (int64_t)(a.ws_bytes - kCounterArea) / part_bytes : 0;
   const bool split = room >= kSmsPlanned;        // (with less than the room asked for no unit is split, on all CTAs)
   // A launch takes up to kMaxBatch sequences, and a line of 31 bits: larger batches go in slices.
-  const int64_t rows = a.max_q * (a.q_heads / a.kv_heads);
-  const double line = (double)a.kv_heads * (double)((rows + kRows - 1) / kRows) *
-                      (double)((a.max_pages * a.page_size + kTile - 1) / kTile + kUnitCost);   // of a sequence, at most
+  const double line = kv_attention_places(a.max_q, a.q_heads, a.kv_heads, a.head_dim, a.max_pages * a.page_size);
   const double fit = 2147483647.0 / line;
-  if (fit < 1.0) return cudaErrorInvalidValue;
+  if (fit < 1.0) return cudaErrorInvalidValue;               // (the entry point has seen to that)
   int64_t slice = a.batch < kMaxBatch ? a.batch : kMaxBatch;
   if (fit < (double)slice) slice = (int64_t)fit;
   for (int64_t b0 = 0; b0 < a.batch; b0 += slice) {
@@ -1083,6 +1081,10 @@ cudaError_t launch_tc_attention(const KvAttentionParams &a, cudaStream_t st) {
 }
 
 }  // namespace
+
+double kv_attention_tc_places(int64_t rows, int64_t kv_heads, int64_t tokens) {
+  return (double)kv_heads * (double)((rows + kRows - 1) / kRows) * (double)((tokens + kTile - 1) / kTile + kUnitCost);
+}
 
 size_t kv_attention_tc_workspace_bytes(int64_t head_dim) {
   return kCounterArea + (size_t)kSmsPlanned * 2 * (size_t)kRows * (size_t)(head_dim + 2) * sizeof(float);

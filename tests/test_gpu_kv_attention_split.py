@@ -4,6 +4,8 @@ import numpy as np
 import pytest
 import torch
 
+from gpu_util import bf16_host, dev, host
+from kv_util import check_attention
 from test_gpu_kv_attention import Problem
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +77,22 @@ def test_a_workspace_that_is_too_small_splits_nothing(lib, seqs, hq, hkv, d):
         got = p.call(lib, t, ws)
         torch.cuda.synchronize()
         assert _equal(got, whole) and not ws.any()
+
+
+@pytest.mark.parametrize("seqs,hq,hkv,d", [([(70, 20), (2, 2)], 64, 8, 128), ([(40, 33)], 64, 8, 64)])
+def test_a_chunk_in_a_table_for_a_million_tokens(lib, seqs, hq, hkv, d):
+    """The size of the table bounds the work that a call may have, counted in
+    the tiles of the form that runs: chunks of 8192 of 64 heads fit."""
+    p = Problem(seqs, hq, hkv, d, 16, seed=15)
+    wide = np.full((len(seqs), (1 << 20) // 16), -1, dtype=np.int32)
+    wide[:, :p.table.shape[1]] = p.table
+    ref = p.reference()
+    t = p.device()
+    out = torch.empty((p.tokens, hq, d), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((p.tokens, hq), device="cuda")
+    n = lib.nvfp4_kv_attention_workspace_bytes(p.tokens, len(seqs), 8192, hq, hkv, d)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    lib.nvfp4_kv_attention(t["q"], hq * d, t["cu"], t["cache"], dev(wide), t["lens"], t["qk"], t["vs"], out, lse,
+                           p.tokens, len(seqs), 8192, hq, hkv, d, p.pages, 16, wide.shape[1], 0, ws, n)
+    torch.cuda.synchronize()
+    check_attention(bf16_host(out), host(lse), ref)
