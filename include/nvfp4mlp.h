@@ -545,7 +545,7 @@ nvfp4_status nvfp4_kv_attention(const uint16_t *q, int64_t q_stride, const int32
                                 int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t pages,
                                 int64_t page_size, int64_t max_pages, int64_t window, void *workspace,
                                 size_t ws_bytes, nvfp4_stream_t stream);
-/* Workspace bytes for nvfp4_kv_attention (0 for invalid arguments).  Host
+/* Workspace bytes for nvfp4_kv_attention (0 for counts that it refuses).  Host
  * only. */
 size_t nvfp4_kv_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t max_q, int64_t q_heads,
                                           int64_t kv_heads, int64_t head_dim);

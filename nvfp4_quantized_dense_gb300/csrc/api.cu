@@ -511,6 +511,11 @@ bool bad_rows(int64_t stride, int64_t heads, int64_t head_dim) {
   return stride % 8 != 0 || stride < heads * head_dim || stride > (int64_t(1) << 31);
 }
 
+// Counts that an attention call does not take.
+bool bad_batch(int64_t tokens, int64_t batch, int64_t max_q, int64_t q_heads) {
+  return batch > 65536 || max_q > (int64_t(1) << 28) || q_heads > 1024 || tokens >= (int64_t(1) << 31) / q_heads;
+}
+
 nvfp4_status check_norm(const uint16_t *x, const uint16_t *residual, const uint16_t *weight,
                         const uint16_t *residual_out, const void *out, int64_t m, int64_t k) {
   if (m < 0 || k <= 0) return NVFP4_ERR_INVALID_ARG;
@@ -588,8 +593,8 @@ nvfp4_status nvfp4_kv_cache_read(const uint8_t *cache, const int64_t *slots, con
 size_t nvfp4_kv_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t max_q, int64_t q_heads,
                                           int64_t kv_heads, int64_t head_dim) {
   if (tokens <= 0 || batch <= 0 || max_q <= 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0) return 0;
-  if (head_dim != 64 && head_dim != 128) return 0;
-  return kv_attention_workspace_bytes(tokens, batch, max_q, q_heads, kv_heads, head_dim);
+  if ((head_dim != 64 && head_dim != 128) || kv_heads > 1024 || bad_batch(tokens, batch, max_q, q_heads)) return 0;
+  return kv_attention_workspace_bytes(max_q, q_heads, kv_heads, head_dim);
 }
 
 nvfp4_status nvfp4_kv_attention(const uint16_t *q, int64_t q_stride, const int32_t *cu_q, const uint8_t *cache,
@@ -603,9 +608,9 @@ nvfp4_status nvfp4_kv_attention(const uint16_t *q, int64_t q_stride, const int32
     return NVFP4_ERR_INVALID_ARG;
   if (nvfp4_status s = check_cache(pages, page_size, kv_heads, head_dim)) return s;
   if (q_heads % kv_heads != 0) return NVFP4_ERR_INVALID_ARG;
-  if (batch > 65536 || max_q > (int64_t(1) << 28) || q_heads > 1024 || tokens >= (int64_t(1) << 31) / q_heads ||
-      max_pages > (int64_t(1) << 30) || max_pages * page_size > (int64_t(1) << 30) ||
-      window >= (int64_t(1) << 31) || bad_rows(q_stride, q_heads, head_dim))
+  if (bad_batch(tokens, batch, max_q, q_heads) || max_pages > (int64_t(1) << 30) ||
+      max_pages * page_size > (int64_t(1) << 30) || window >= (int64_t(1) << 31) ||
+      bad_rows(q_stride, q_heads, head_dim))
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   // a sequence's share of the work is counted in 31 bits
   if (kv_attention_places(max_q, q_heads, kv_heads, head_dim, max_pages * page_size) > 2147483647.0)

@@ -206,8 +206,7 @@ struct KvAttentionParams {
   size_t ws_bytes;
   uint32_t wait_limit;
 };
-size_t kv_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads,
-                                    int64_t head_dim);
+size_t kv_attention_workspace_bytes(int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 // Places of one sequence on the line of work that the form for these sizes
 // cuts, at most; the kernels count a launch's in 31 bits.  tokens: the block
 // table's capacity.

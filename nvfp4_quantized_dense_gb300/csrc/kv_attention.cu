@@ -749,8 +749,7 @@ double kv_attention_places(int64_t max_q, int64_t q_heads, int64_t kv_heads, int
   return (double)kv_heads * (double)((rows + 31) / 32) * (double)((tokens + kStep - 1) / kStep + unit_cost(tile_groups(rows)));
 }
 
-size_t kv_attention_workspace_bytes(int64_t, int64_t, int64_t max_q, int64_t q_heads, int64_t kv_heads,
-                                    int64_t head_dim) {
+size_t kv_attention_workspace_bytes(int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
   const int64_t rows = max_q * (q_heads / kv_heads);
   if (rows > tc_rows(head_dim)) return kv_attention_tc_workspace_bytes(head_dim);
   const int nq = tile_groups(rows);

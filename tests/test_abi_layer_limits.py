@@ -37,3 +37,13 @@ def test_sizes_that_fit(lib, max_q, hq, hkv, d, table):
     (33, 256, 256, 128, 1 << 30)])
 def test_sizes_that_do_not(lib, max_q, hq, hkv, d, table):
     assert _attend(lib, max_q, hq, hkv, d, table) == SHAPE
+
+
+def test_workspace_of_sizes_that_are_refused(lib):
+    """0 bytes for what the call would refuse, however large the numbers."""
+    f = nv.nvfp4_kv_attention_workspace_bytes
+    assert f(4, 4, 1, 8, 2, 128) > 65536
+    for bad in ((4, 65537, 1, 8, 2, 128), (1 << 31, 4, 1, 8, 2, 128), (4, 4, (1 << 28) + 1, 8, 2, 128),
+                (4, 4, 1 << 62, 8, 2, 128), (4, 4, 1, 2048, 2, 128), (4, 4, 1, 1 << 62, 1 << 61, 128),
+                (4, 4, 1, 8, 8, 256)):
+        assert f(*bad) == 0, bad
