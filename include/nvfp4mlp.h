@@ -432,7 +432,8 @@ nvfp4_status nvfp4_gemm_decode_noalloc(const uint8_t *a_fp4, const uint8_t *a_sf
 /* ---------------------------------------------------------------------------
  * The decoder layer around the MLP: norm, key/value cache, attention.  The
  * source pages have no counterpart to these calls; they hand their results
- * over in the formats of the calls above.
+ * over in the formats of the calls above.  With no rows or tokens (m, n, tokens
+ * == 0) they launch nothing, and any pointer may be NULL.
  * ------------------------------------------------------------------------- */
 
 /* Residual addition + root-mean-square norm + NVFP4 quantize, in one pass:
@@ -484,8 +485,7 @@ size_t nvfp4_kv_cache_bytes(int64_t pages, int64_t page_size, int64_t kv_heads, 
  *              negative or past the cache are skipped.  Two tokens of one
  *              call must not have the same slot.
  *   k_global_scale, v_global_scale  fp32 [1]: gs of nvfp4_quantize, whose
- *              recipe each 16-block follows exactly
- * n == 0 is valid and launches nothing. */
+ *              recipe each 16-block follows exactly */
 nvfp4_status nvfp4_kv_cache_write(const uint16_t *k, const uint16_t *v, int64_t k_stride, int64_t v_stride,
                                   const int64_t *slots, const float *k_global_scale, const float *v_global_scale,
                                   uint8_t *cache, int64_t n, int64_t kv_heads, int64_t head_dim, int64_t pages,
@@ -514,7 +514,8 @@ nvfp4_status nvfp4_kv_cache_read(const uint8_t *cache, const int64_t *slots, con
  *   cu_q         int32 [batch + 1] DEVICE: sequence b's queries are tokens
  *                cu_q[b] .. cu_q[b+1] - 1 (ascending, from 0 to tokens); NULL:
  *                max_q queries each (tokens == batch * max_q)
- *   max_q        the largest q_len (HOST); no sequence may have more
+ *   max_q        the largest q_len (HOST); no sequence may have more (0 only
+ *                with tokens == 0)
  *   block_table  int32 [batch, max_pages] DEVICE: the pages of each sequence
  *                in order; entries past a sequence's length are not used.  The
  *                tokens of an entry outside [0, pages) are not attended to.

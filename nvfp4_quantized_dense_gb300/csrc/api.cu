@@ -506,6 +506,9 @@ nvfp4_status check_cache(int64_t pages, int64_t page_size, int64_t kv_heads, int
   return NVFP4_OK;
 }
 
+// (The calls below take NULL for a tensor that a call on no rows, tokens or
+// sequences does not use: so an empty tensor's address often is.)
+
 // Token counts and strides of bf16 [n, heads, head_dim] tensors.
 bool bad_rows(int64_t stride, int64_t heads, int64_t head_dim) {
   return stride % 8 != 0 || stride < heads * head_dim || stride > (int64_t(1) << 31);
@@ -533,7 +536,7 @@ nvfp4_status add_rms_norm_nvfp4_quantize(const uint16_t *x, const uint16_t *resi
                                          const float *eps, const float *global_scale, uint16_t *residual_out,
                                          uint8_t *out_fp4, uint8_t *out_sf, nvfp4_sf_layout sf_layout, int64_t m,
                                          int64_t k, nvfp4_stream_t stream) {
-  if (!x || !weight || !eps || !global_scale || !out_fp4 || !out_sf) return NVFP4_ERR_INVALID_ARG;
+  if (m != 0 && (!x || !weight || !eps || !global_scale || !out_fp4 || !out_sf)) return NVFP4_ERR_INVALID_ARG;
   if (sf_layout != NVFP4_SF_LINEAR && sf_layout != NVFP4_SF_SWIZZLED_128x4) return NVFP4_ERR_INVALID_ARG;
   if (nvfp4_status s = check_norm(x, residual, weight, residual_out, out_fp4, m, k)) return s;
   if (nvfp4_status s = check_arch()) return s;
@@ -546,7 +549,7 @@ nvfp4_status add_rms_norm_fp8_quantize(const uint16_t *x, const uint16_t *residu
                                        const float *eps, uint16_t *residual_out, uint8_t *out_fp8,
                                        float *out_scale, int64_t group, int64_t m, int64_t k,
                                        nvfp4_stream_t stream) {
-  if (!x || !weight || !eps || !out_fp8 || !out_scale) return NVFP4_ERR_INVALID_ARG;
+  if (m != 0 && (!x || !weight || !eps || !out_fp8 || !out_scale)) return NVFP4_ERR_INVALID_ARG;
   if (group != 0 && group != 128) return NVFP4_ERR_INVALID_ARG;
   if (nvfp4_status s = check_norm(x, residual, weight, residual_out, out_fp8, m, k)) return s;
   if (group == 128 && k % 128 != 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
@@ -565,7 +568,8 @@ nvfp4_status nvfp4_kv_cache_write(const uint16_t *k, const uint16_t *v, int64_t 
                                   const int64_t *slots, const float *k_global_scale, const float *v_global_scale,
                                   uint8_t *cache, int64_t n, int64_t kv_heads, int64_t head_dim, int64_t pages,
                                   int64_t page_size, nvfp4_stream_t stream) {
-  if (!k || !v || !slots || !k_global_scale || !v_global_scale || !cache || n < 0) return NVFP4_ERR_INVALID_ARG;
+  if (n < 0 || (n != 0 && (!k || !v || !slots || !k_global_scale || !v_global_scale || !cache)))
+    return NVFP4_ERR_INVALID_ARG;
   if (nvfp4_status s = check_cache(pages, page_size, kv_heads, head_dim)) return s;
   if (bad_rows(k_stride, kv_heads, head_dim) || bad_rows(v_stride, kv_heads, head_dim) || !aligned16(k) ||
       !aligned16(v) || !aligned16(cache) || n >= (int64_t(1) << 31))
@@ -580,7 +584,8 @@ nvfp4_status nvfp4_kv_cache_read(const uint8_t *cache, const int64_t *slots, con
                                  const float *v_scale, uint16_t *k_out, uint16_t *v_out, int64_t n,
                                  int64_t kv_heads, int64_t head_dim, int64_t pages, int64_t page_size,
                                  nvfp4_stream_t stream) {
-  if (!cache || !slots || !k_scale || !v_scale || !k_out || !v_out || n < 0) return NVFP4_ERR_INVALID_ARG;
+  if (n < 0 || (n != 0 && (!cache || !slots || !k_scale || !v_scale || !k_out || !v_out)))
+    return NVFP4_ERR_INVALID_ARG;
   if (nvfp4_status s = check_cache(pages, page_size, kv_heads, head_dim)) return s;
   if (!aligned16(cache) || !aligned16(k_out) || !aligned16(v_out) || n >= (int64_t(1) << 31))
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
@@ -603,8 +608,9 @@ nvfp4_status nvfp4_kv_attention(const uint16_t *q, int64_t q_stride, const int32
                                 int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t pages,
                                 int64_t page_size, int64_t max_pages, int64_t window, void *workspace,
                                 size_t ws_bytes, nvfp4_stream_t stream) {
-  if (!q || !cache || !block_table || !seq_lens || !qk_scale || !v_scale || !out) return NVFP4_ERR_INVALID_ARG;
-  if (tokens < 0 || batch < 0 || max_q <= 0 || q_heads <= 0 || max_pages <= 0 || window < 0)
+  if (tokens < 0 || batch < 0 || max_q < 0 || q_heads <= 0 || max_pages <= 0 || window < 0)
+    return NVFP4_ERR_INVALID_ARG;
+  if (tokens != 0 && (!q || !cache || !block_table || !seq_lens || !qk_scale || !v_scale || !out || max_q == 0))
     return NVFP4_ERR_INVALID_ARG;
   if (nvfp4_status s = check_cache(pages, page_size, kv_heads, head_dim)) return s;
   if (q_heads % kv_heads != 0) return NVFP4_ERR_INVALID_ARG;
@@ -613,7 +619,7 @@ nvfp4_status nvfp4_kv_attention(const uint16_t *q, int64_t q_stride, const int32
       bad_rows(q_stride, q_heads, head_dim))
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   // a sequence's share of the work is counted in 31 bits
-  if (kv_attention_places(max_q, q_heads, kv_heads, head_dim, max_pages * page_size) > 2147483647.0)
+  if (max_q != 0 && kv_attention_places(max_q, q_heads, kv_heads, head_dim, max_pages * page_size) > 2147483647.0)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (!cu_q && tokens != batch * max_q) return NVFP4_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || (workspace && !aligned16(workspace)))

@@ -47,3 +47,24 @@ def test_workspace_of_sizes_that_are_refused(lib):
                 (4, 4, 1 << 62, 8, 2, 128), (4, 4, 1, 2048, 2, 128), (4, 4, 1, 1 << 62, 1 << 61, 128),
                 (4, 4, 1, 8, 8, 256)):
         assert f(*bad) == 0, bad
+
+
+def test_calls_on_nothing(lib):
+    """No rows, tokens or sequences: the tensors may have no memory (an empty
+    tensor's address is NULL), and the answer is never a refusal."""
+    refused = (INV, SHAPE)
+    z = None
+    assert lib.add_rms_norm_nvfp4_quantize(z, z, FAKE, FAKE, FAKE, z, z, z, 0, 0, 256, None) not in refused
+    assert lib.add_rms_norm_nvfp4_quantize(z, z, z, z, z, z, z, z, 0, 0, 256, None) not in refused
+    assert lib.add_rms_norm_fp8_quantize(z, z, FAKE, FAKE, z, z, z, 128, 0, 256, None) not in refused
+    assert lib.nvfp4_kv_cache_write(z, z, 256, 256, z, FAKE, FAKE, FAKE, 0, 2, 128, 3, 16, None) not in refused
+    assert lib.nvfp4_kv_cache_read(FAKE, z, FAKE, FAKE, z, z, 0, 2, 128, 3, 16, None) not in refused
+    attend = lib.nvfp4_kv_attention
+    #              q  qs    cu    cache table lens  qk    vs    out lse tok b mq hq hkv d  pages page maxp win ws ws_b st
+    assert attend(z, 1024, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, z, z, 0, 4, 0, 8, 2, 128, 9, 16, 3, 0, z, 0, None) not in refused
+    assert attend(z, 1024, z, FAKE, z, z, FAKE, FAKE, z, z, 0, 0, 1, 8, 2, 128, 9, 16, 3, 0, z, 0, None) not in refused
+    # what does not depend on the number of tokens is checked all the same
+    assert lib.add_rms_norm_nvfp4_quantize(z, z, FAKE, FAKE, FAKE, z, z, z, 0, 0, 250, None) == SHAPE
+    assert lib.nvfp4_kv_cache_write(z, z, 256, 256, z, FAKE, FAKE, FAKE, 0, 2, 96, 3, 16, None) == SHAPE
+    assert attend(z, 1024, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, z, z, 0, 4, -1, 8, 2, 128, 9, 16, 3, 0, z, 0, None) == INV
+    assert attend(z, 1024, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, z, z, 0, 4, 1, 8, 3, 128, 9, 16, 3, 0, z, 0, None) == INV
