@@ -99,10 +99,9 @@ def load(path=LIB_PATH):
 
 
 def _ptr(x):
-    try:
-        return x.data_ptr()
-    except AttributeError:      # None or an integer address
+    if x is None or type(x) is int:
         return x
+    return x.data_ptr()     # (an AttributeError for anything that is not a tensor)
 
 
 _raw_stream = _device = None

@@ -68,3 +68,12 @@ def test_calls_on_nothing(lib):
     assert lib.nvfp4_kv_cache_write(z, z, 256, 256, z, FAKE, FAKE, FAKE, 0, 2, 96, 3, 16, None) == SHAPE
     assert attend(z, 1024, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, z, z, 0, 4, -1, 8, 2, 128, 9, 16, 3, 0, z, 0, None) == INV
     assert attend(z, 1024, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, z, z, 0, 4, 1, 8, 3, 128, 9, 16, 3, 0, z, 0, None) == INV
+
+
+@pytest.mark.parametrize("bad", [b"0123456789abcdef", "text", bytearray(16), 1.5, np.zeros(4, np.float32), [1]], ids=lambda x: type(x).__name__)
+def test_pointers_are_tensors_integers_or_none(lib, bad):
+    """Host memory never reaches a kernel by way of the binding."""
+    with pytest.raises(AttributeError):
+        nv.nvfp4_kv_cache_write(bad, FAKE, 256, 256, FAKE, FAKE, FAKE, FAKE, 0, 2, 96, 3, 16, stream=0)
+    with pytest.raises(AttributeError):
+        nv.nvfp4_quantize(bad, 0, 250, FAKE, FAKE, FAKE, stream=0)
