@@ -452,7 +452,8 @@ nvfp4_status add_rms_norm_nvfp4_quantize(const uint16_t *x, const uint16_t *resi
 
 /* The same norm with an 8-bit output: E4M3 values (e4m3fn) and fp32 scales,
  * one per row (group == 0) or per `group` == 128 consecutive elements:
- *   s = fp32(amax / 448) over the row or group (1 where amax is 0)
+ *   s = fp32(amax / 448) over the row or group (1 where amax is 0, else at
+ *       least 2^-126)
  *   out_fp8 = E4M3( fp32(y * fp32(1 / s)) )      RNE, saturating
  * so that out_fp8 * s stands for y.
  *   out_fp8    uint8 [m, k];  out_scale fp32 [m] or [m, k/128]

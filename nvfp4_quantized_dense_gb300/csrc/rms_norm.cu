@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_norm_kernel(const NormArgs 
       for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     }
     if (j >= cols) continue;
-    const float s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f, inv = __fdiv_rn(1.0f, s);
+    // (not below the smallest normal number: 1 / s would be infinite, and a zero times it NaN)
+    const float s = amax > 0.0f ? fmaxf(__fdiv_rn(amax, 448.0f), 1.17549435e-38f) : 1.0f, inv = __fdiv_rn(1.0f, s);
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
