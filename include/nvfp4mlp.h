@@ -439,7 +439,8 @@ nvfp4_status nvfp4_gemm_decode_noalloc(const uint8_t *a_fp4, const uint8_t *a_sf
 /* Residual addition + root-mean-square norm + NVFP4 quantize, in one pass:
  *   r = bf16(x + residual)                       (r = x when residual is NULL)
  *   y = r * rsqrt(mean(r^2) + eps) * weight      in fp32, not rounded to bf16
- *   out_fp4, out_sf = y quantized exactly as nvfp4_quantize
+ *   out_fp4, out_sf = y quantized exactly as nvfp4_quantize; a 16-block with a
+ *   NaN (a NaN in x or residual makes all of its row) gets the scale 0x7F, NaN
  *   x, residual    bf16 [m, k];  weight bf16 [k];  eps fp32 [1] DEVICE
  *   global_scale   fp32 [1]: the next GEMM's input global scale
  *   residual_out   bf16 [m, k]: r (may be NULL; may equal x or residual)
@@ -455,7 +456,8 @@ nvfp4_status add_rms_norm_nvfp4_quantize(const uint16_t *x, const uint16_t *resi
  *   s = fp32(amax / 448) over the row or group (1 where amax is 0, else at
  *       least 2^-126)
  *   out_fp8 = E4M3( fp32(y * fp32(1 / s)) )      RNE, saturating
- * so that out_fp8 * s stands for y.
+ * so that out_fp8 * s stands for y.  A NaN of y is E4M3's NaN and does not
+ * count for amax.
  *   out_fp8    uint8 [m, k];  out_scale fp32 [m] or [m, k/128]
  * Requires as above, and k % 128 == 0 for group == 128. */
 nvfp4_status add_rms_norm_fp8_quantize(const uint16_t *x, const uint16_t *residual, const uint16_t *weight,

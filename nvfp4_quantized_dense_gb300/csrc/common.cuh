@@ -64,12 +64,10 @@ __device__ __forceinline__ float bf16_hi(uint32_t two) { return __uint_as_float(
 
 // NVFP4 quantize of one 16-element block held in registers, in the order
 // the API documents: s = fp32(amax/6)*gs, SF = E4M3(s), r = gs/SF, codes of
-// x*r.  Returns the scale byte; writes the 8 packed code bytes to lo/hi.
-__device__ __forceinline__ uint32_t quantize_block16(const float (&x)[16], float gs, uint32_t &lo,
+// x*r, amax the block's largest magnitude.  Returns the scale byte; writes the
+// 8 packed code bytes to lo/hi.
+__device__ __forceinline__ uint32_t quantize_block16(const float (&x)[16], float amax, float gs, uint32_t &lo,
                                                      uint32_t &hi) {
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
   const float s = __fmul_rn(__fdiv_rn(amax, 6.0f), gs);
   const uint32_t sf = e4m3_encode_satfinite(s);
   const float r = (sf == 0u) ? 0.0f : __fdiv_rn(gs, e4m3_decode(sf));
@@ -79,6 +77,14 @@ __device__ __forceinline__ uint32_t quantize_block16(const float (&x)[16], float
   lo = e2m1_pack8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
   hi = e2m1_pack8(v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]);
   return sf;
+}
+
+// The same with amax taken here; a NaN does not count for it.
+__device__ __forceinline__ uint32_t quantize_block16(const float (&x)[16], float gs, uint32_t &lo, uint32_t &hi) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+  return quantize_block16(x, amax, gs, lo, hi);
 }
 
 // Byte offset of block scale (row r, scale column j) in the 128x4 swizzled

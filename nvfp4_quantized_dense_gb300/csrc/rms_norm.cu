@@ -96,6 +96,15 @@ __device__ __forceinline__ void norm16(const uint32_t (&r)[8], const uint16_t *w
   }
 }
 
+// Largest magnitude of a block, NaN where one is: it makes the block's scale
+// E4M3's NaN (fmaxf would drop it, and make zeros of a row that holds one).
+__device__ __forceinline__ float amax16_nan(const float (&y)[16]) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(y[i])));
+  return amax;
+}
+
 __device__ __forceinline__ float amax16(const float (&y)[16]) {
   float amax = 0.0f;
 #pragma unroll
@@ -165,7 +174,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_norm_kernel(const NormArgs 
         float y[16];
         norm16(r[c], a.weight + (int64_t)j * 16, rstd, y);
         uint32_t lo, hi;
-        sf = quantize_block16(y, gs, lo, hi);
+        sf = quantize_block16(y, amax16_nan(y), gs, lo, hi);
         *reinterpret_cast<uint2 *>(a.out + row * (a.k >> 1) + (int64_t)j * 8) = make_uint2(lo, hi);
       }
       if (a.swizzled) {

@@ -43,3 +43,55 @@ def test_fp8_scales_of_tiny_values(lib, group, size, k):
     # E4M3: half a step is 2^-4 of a normal value and 2^-10 of a subnormal one;
     # the scale's own rounding moves value and scale together
     assert (np.abs(v * scale - y) <= np.maximum(np.abs(y) * 2.0 ** -4, scale * 2.0 ** -10) * 1.001).all()
+
+
+def _norm_nvfp4(lib, x, weight, layout):
+    m, k = x.shape
+    q = torch.zeros((m, k // 2), dtype=torch.uint8, device="cuda")
+    sf = torch.zeros(lib.nvfp4_sf_bytes(m, k, layout), dtype=torch.uint8, device="cuda")
+    lib.add_rms_norm_nvfp4_quantize(x, None, weight, scalar(1e-6), scalar(448.0), None, q, sf, layout, m, k)
+    torch.cuda.synchronize()
+    return q, sf
+
+
+@pytest.mark.parametrize("k", [16, 256, 5120, 16384])
+@pytest.mark.parametrize("m", [3, 200])
+def test_nan_in_a_norm_is_not_lost(lib, m, k):
+    """A NaN makes its row NaN, as a scale of 0x7F in every block of it, and no
+    other row moves; a NaN weight the blocks of its column."""
+    x, weight = _rows(m, k, 6), torch.ones(k, dtype=torch.bfloat16, device="cuda")
+    q0, s0 = _norm_nvfp4(lib, x, weight, lib.SF_LINEAR)
+    s0 = s0.reshape(m, -1)
+    x[1, k // 2] = NAN
+    q, s = _norm_nvfp4(lib, x, weight, lib.SF_LINEAR)
+    s = s.reshape(m, -1)
+    keep = torch.arange(m, device="cuda") != 1
+    assert (s[1] == 0x7F).all()
+    assert torch.equal(q[keep], q0[keep]) and torch.equal(s[keep], s0[keep])
+    swizzled = _norm_nvfp4(lib, x, weight, lib.SF_SWIZZLED_128x4)[1]
+    assert int((swizzled == 0x7F).sum()) == k // 16
+    x = _rows(m, k, 6)
+    weight[k - 1] = NAN
+    q, s = _norm_nvfp4(lib, x, weight, lib.SF_LINEAR)
+    s = s.reshape(m, -1)
+    assert (s[:, -1] == 0x7F).all() and torch.equal(s[:, :-1], s0[:, :-1]) and torch.equal(q[:, :k // 2 - 8], q0[:, :k // 2 - 8])
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_nan_in_an_fp8_norm(lib, group):
+    """E4M3 has a NaN of its own: the row's values are it, its scales 1; a NaN
+    weight is its column's values, and no scale's."""
+    x, weight = _rows(4, 512, 7), torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    weight[7] = 0
+    q0, s0 = _norm_fp8(lib, x, weight, group)
+    x[2, 300] = NAN
+    q, s = _norm_fp8(lib, x, weight, group)
+    assert torch.isnan(q[2].view(torch.float8_e4m3fn).float()).all() and (s[2] == 1).all()
+    keep = torch.arange(4, device="cuda") != 2
+    assert torch.equal(q[keep], q0[keep]) and torch.equal(s[keep], s0[keep])
+    x = _rows(4, 512, 7)
+    weight[7] = NAN
+    q, s = _norm_fp8(lib, x, weight, group)
+    assert torch.isnan(q[:, 7].view(torch.float8_e4m3fn).float()).all() and torch.equal(s, s0)
+    q[:, 7] = q0[:, 7]
+    assert torch.equal(q, q0)
