@@ -95,3 +95,32 @@ def test_nan_in_an_fp8_norm(lib, group):
     assert torch.isnan(q[:, 7].view(torch.float8_e4m3fn).float()).all() and torch.equal(s, s0)
     q[:, 7] = q0[:, 7]
     assert torch.equal(q, q0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_cache_write_of_what_is_not_finite(lib, d):
+    """Each block as nvfp4_quantize makes it: a NaN does not count for the
+    block's largest magnitude, and the cache holds finite numbers only."""
+    n, heads, page = 37, 2, 16
+    k, v = _rows(n, heads * d, 8), _rows(n, heads * d, 9)
+    k[1, 3], k[2, 16:32], v[3, 5], v[4, 16:32] = NAN, NAN, NAN, NAN
+    k[5, 7], v[6, 8], k[7], v[7] = float("inf"), -float("inf"), NAN, NAN
+    slots = torch.randperm(3 * page, device="cuda")[:n]
+    gs = scalar(448.0)
+    cache = torch.zeros(lib.nvfp4_kv_cache_bytes(3, page, heads, d), dtype=torch.uint8, device="cuda")
+    lib.nvfp4_kv_cache_write(k, v, heads * d, heads * d, slots, gs, gs, cache, n, heads, d, 3, page)
+    rec = cache.reshape(3, heads, 1, 18 * d)[slots // page, :, 0].reshape(n * heads, 18 * d).long()
+    tok = (slots % 16).repeat_interleave(heads)[:, None]
+    b, x = torch.arange(d // 16, device="cuda"), torch.arange(d // 2, device="cuda")
+    got = [torch.gather(rec, 1, at) for at in (tok * (d // 2) + x, 8 * d + tok * (d // 16) + b,
+                                               9 * d + (x // 8 * 16 + tok) * 8 + x % 8, 17 * d + b * 16 + tok)]
+    for (codes, sf), t in ((got[:2], k), (got[2:], v)):
+        q = torch.zeros((n * heads, d // 2), dtype=torch.uint8, device="cuda")
+        s = torch.zeros((n * heads, d // 16), dtype=torch.uint8, device="cuda")
+        lib.nvfp4_quantize(t.reshape(n * heads, d), n * heads, d, gs, q, s, lib.SF_LINEAR)
+        assert torch.equal(codes, q.long()) and torch.equal(sf, s.long())
+        assert ((sf & 0x7F) != 0x7F).all()
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    lib.nvfp4_kv_cache_read(cache, slots, 1 / gs, 1 / gs, ko, vo, n, heads, d, 3, page)
+    torch.cuda.synchronize()
+    assert torch.isfinite(ko.float()).all() and torch.isfinite(vo.float()).all()
