@@ -468,9 +468,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NQ>::CTAS)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
           top = fmaxf(top, m[n][j]);
-          const float ref = top == -INFINITY ? 0.0f : top * sc[n][j];
+          const float base = top == -INFINITY ? 0.0f : top, ref = base * sc[n][j];
           moved |= top != m[n][j];
-          keep[n][j] = exp2_fast(fmaf(m[n][j], sc[n][j], -ref));
+          // (1 exactly where the maximum stays: m * sc - ref would be ref's
+          // rounding, and the sum, unlike O, takes the factor at every step)
+          keep[n][j] = exp2_fast((m[n][j] - base) * sc[n][j]);
           m[n][j] = top;
           float sum = 0.0f;
 #pragma unroll
