@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NQ>::CTAS)
       bool moved = false;
       float keep[NQ][2];
 #pragma unroll
-      for (int n = 0; n < NQ; ++n)
+      for (int n = 0; n < NQ; ++n) {
+        float base[2];                            // what the exponentials refer to
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float top = fmaxf(fmaxf(s[n][0][j], s[n][0][j + 2]), fmaxf(s[n][1][j], s[n][1][j + 2]));
@@ -468,22 +469,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NQ>::CTAS)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
           top = fmaxf(top, m[n][j]);
-          const float base = top == -INFINITY ? 0.0f : top, ref = base * sc[n][j];
+          base[j] = top == -INFINITY ? 0.0f : top;
           moved |= top != m[n][j];
-          // (1 exactly where the maximum stays: m * sc - ref would be ref's
-          // rounding, and the sum, unlike O, takes the factor at every step)
-          keep[n][j] = exp2_fast((m[n][j] - base) * sc[n][j]);
+          // (1 exactly where the maximum stays: the sum, unlike O, takes the factor at every step)
+          keep[n][j] = exp2_fast((m[n][j] - base[j]) * sc[n][j]);
           m[n][j] = top;
-          float sum = 0.0f;
-#pragma unroll
-          for (int rec = 0; rec < 2; ++rec)
-#pragma unroll
-            for (int i = j; i < 4; i += 2) {
-              s[n][rec][i] = exp2_fast(fmaf(s[n][rec][i], sc[n][j], kShift - ref));
-              sum += s[n][rec][i];
-            }
-          l[n][j] = l[n][j] * keep[n][j] + sum;
         }
+        // The difference first, then the scale: s * sc - base * sc would be off
+        // by the product's rounding, without limit for large scores.  (Both
+        // rows of a lane in one instruction.)
+        const uint64_t minus = pack2(-base[0], -base[1]), sc2 = pack2(sc[n][0], sc[n][1]), shift2 = pack2(kShift, kShift);
+        uint64_t sum2 = 0;
+#pragma unroll
+        for (int rec = 0; rec < 2; ++rec)
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            unpack2(fma2(add2(pack2(s[n][rec][i], s[n][rec][i + 1]), minus), sc2, shift2), s[n][rec][i], s[n][rec][i + 1]);
+            s[n][rec][i] = exp2_fast(s[n][rec][i]), s[n][rec][i + 1] = exp2_fast(s[n][rec][i + 1]);
+            sum2 = add2(sum2, pack2(s[n][rec][i], s[n][rec][i + 1]));
+          }
+        float sum[2];
+        unpack2(sum2, sum[0], sum[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) l[n][j] = l[n][j] * keep[n][j] + sum[j];
+      }
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll

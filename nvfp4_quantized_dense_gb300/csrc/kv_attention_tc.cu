@@ -60,6 +60,8 @@
 #include "kv_layout.cuh"
 #include "tc_ptx.cuh"
 
+#include <type_traits>
+
 namespace nvfp4 {
 namespace {
 
@@ -71,7 +73,7 @@ constexpr int kRows = 2 * kTile;             // rows of a unit
 constexpr int kMinTiles = 4;                 // cached tiles worth a CTA
 constexpr int kUnitCost = 4;                 // what a unit's beginning and end cost, in tiles (nine mixed sequences: 3, 4, 5 give 87, 85, 85 us)
 constexpr int kMaxBatch = 1024;
-constexpr float kShift = 14.0f, kSlack = 1.9f;
+constexpr float kShift = 14.0f, kSlack = 1.9f, kFar = 65536.0f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kDrainPolls = 1u << 22, kPollNs = 20000;
 constexpr int kSmsPlanned = 152;
@@ -199,30 +201,6 @@ struct Walk {
   __device__ __forceinline__ int rows() const { return min(u.qn * group - u.tile * kRows, kRows); }
 };
 
-// Pairs of floats in one instruction each (sm_100 and later).
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -525,93 +503,114 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int end_c = min(hi + 1, w.len) - base_t, lo_c = win > 0 ? hi - win + 1 - base_t : -1;
         const int part_hi = min(p0 + 1, w.len) - base_t;
         const int part_lo = win > 0 ? p1 - win + 1 - base_t : -1;
-        for (int j = 0; j < count; ++j, ++step) {
-          const bool got = wait(&s_sfull[t], step & 1);
-          if (__any_sync(0xffffffffu, !got)) {
-            give_up();
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t valid = s_valid[(tile_no + j) & 3];
-          const bool masked = valid != 0x03030303u || (j + 1) * kTile > part_hi || j * kTile < part_lo;
-          // ---- the row's scores, all in registers, and their maximum
-          uint32_t s[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) ptx::tmem_ld32(s_col + 32 * c, s[c]);
-          ptx::tmem_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int col = 32 * c + i;
-                if (col >= end_c - j * kTile || col < lo_c - j * kTile || !((valid >> (c * 8 + (i >> 4))) & 1)) s[c][i] = 0xff800000u;
-              }
-          }
-          float top4[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            top4[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-            for (int i = 1; i + 1 < 32; i += 2)
-              top4[c] = max3(top4[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
-            top4[c] = fmaxf(top4[c], __uint_as_float(s[c][31]));
-          }
-          const float mx = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-          bool grow = false;
-          float keep = 1.0f;
-          if (j == 0) {
-            m = mx;
-          } else if (mx * sc > (m == -INFINITY ? -INFINITY : m * sc + kSlack)) {
-            grow = true;
-            keep = m == -INFINITY ? 0.0f : exp2_fast((m - mx) * sc);
-            m = mx;
-            l *= keep;
-          }
-          // ---- probabilities over the scores' own columns
-          const float bias = kShift - (m == -INFINITY ? 0.0f : m * sc);
-          const uint64_t sc2 = pack2(sc, sc), bias2 = pack2(bias, bias);
-          uint64_t sum2[2] = {0, 0};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint64_t x = fma2(pack2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), sc2, bias2);
-              float e0, e1;
-              unpack2(x, e0, e1);
-              e0 = exp2_fast(e0), e1 = exp2_fast(e1);
-              sum2[i & 1] = add2(sum2[i & 1], pack2(e0, e1));
-              p[i] = f16x2(e0, e1);
+        auto tiles = [&](auto far_rows) {
+          for (int j = 0; j < count; ++j, ++step) {
+            const bool got = wait(&s_sfull[t], step & 1);
+            if (__any_sync(0xffffffffu, !got)) {
+              give_up();
+              return false;
             }
-            ptx::tmem_st16(s_col + 16 * c, p);
-          }
-          float l0, l1;
-          unpack2(add2(sum2[0], sum2[1]), l0, l1);
-          l += l0 + l1;
-          if (__any_sync(0xffffffffu, grow)) {   // O follows the reference (last: the scores' registers are free now)
-            const uint64_t keep2 = pack2(keep, keep);
-            uint32_t o[D / 32][32];
+            ptx::tc_fence_after();
+            const uint32_t valid = s_valid[(tile_no + j) & 3];
+            const bool masked = valid != 0x03030303u || (j + 1) * kTile > part_hi || j * kTile < part_lo;
+            // ---- the row's scores, all in registers, and their maximum
+            uint32_t s[4][32];
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) ptx::tmem_ld32(o_col + 32 * c, o[c]);
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld32(s_col + 32 * c, s[c]);
             ptx::tmem_wait_ld();
+            if (masked) {
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+              for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float x0, x1;
-                unpack2(mul2(pack2(__uint_as_float(o[c][i]), __uint_as_float(o[c][i + 1])), keep2), x0, x1);
-                o[c][i] = __float_as_uint(x0), o[c][i + 1] = __float_as_uint(x1);
-              }
-              ptx::tmem_st32(o_col + 32 * c, o[c]);
+                for (int i = 0; i < 32; ++i) {
+                  const int col = 32 * c + i;
+                  if (col >= end_c - j * kTile || col < lo_c - j * kTile || !((valid >> (c * 8 + (i >> 4))) & 1)) s[c][i] = 0xff800000u;
+                }
             }
+            float top4[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              top4[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+              for (int i = 1; i + 1 < 32; i += 2)
+                top4[c] = max3(top4[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+              top4[c] = fmaxf(top4[c], __uint_as_float(s[c][31]));
+            }
+            const float mx = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+            bool grow = false;
+            float keep = 1.0f;
+            if (j == 0) {
+              m = mx;
+            } else if ((mx - m) * sc > kSlack) {   // (infinite where m is -inf, NaN where both are)
+              grow = true;
+              keep = m == -INFINITY ? 0.0f : exp2_fast((m - mx) * sc);
+              m = mx;
+              l *= keep;
+            }
+            // ---- probabilities over the scores' own columns
+            const float ref0 = m == -INFINITY ? 0.0f : __fmul_rn(m, sc);       // (the same roundings in both loops)
+            float bias = __fadd_rn(kShift, -ref0);
+            if constexpr (decltype(far_rows)::value) {
+              const bool far = fabsf(ref0) >= kFar;
+              const uint64_t minus = pack2(far ? -m : 0.0f, far ? -m : 0.0f);
+              if (far) bias = kShift;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float x0, x1;
+                  unpack2(add2(pack2(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])), minus), x0, x1);
+                  s[c][i] = __float_as_uint(x0), s[c][i + 1] = __float_as_uint(x1);
+                }
+            }
+            const uint64_t sc2 = pack2(sc, sc), bias2 = pack2(bias, bias);
+            uint64_t sum2[2] = {0, 0};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t p[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const uint64_t x = fma2(pack2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), sc2, bias2);
+                float e0, e1;
+                unpack2(x, e0, e1);
+                e0 = exp2_fast(e0), e1 = exp2_fast(e1);
+                sum2[i & 1] = add2(sum2[i & 1], pack2(e0, e1));
+                p[i] = f16x2(e0, e1);
+              }
+              ptx::tmem_st16(s_col + 16 * c, p);
+            }
+            float l0, l1;
+            unpack2(add2(sum2[0], sum2[1]), l0, l1);
+            l += l0 + l1;
+            if (__any_sync(0xffffffffu, grow)) {   // O follows the reference (last: the scores' registers are free now)
+              const uint64_t keep2 = pack2(keep, keep);
+              uint32_t o[D / 32][32];
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) ptx::tmem_ld32(o_col + 32 * c, o[c]);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float x0, x1;
+                  unpack2(mul2(pack2(__uint_as_float(o[c][i]), __uint_as_float(o[c][i + 1])), keep2), x0, x1);
+                  o[c][i] = __float_as_uint(x0), o[c][i + 1] = __float_as_uint(x1);
+                }
+                ptx::tmem_st32(o_col + 32 * c, o[c]);
+              }
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s_pfull[t]);
           }
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&s_pfull[t]);
-        }
+          return true;
+        };
+        // s * sc + bias is off by the rounding of m * sc.  Rows where that could
+        // be a good part of 1 take the difference s - m first, in a loop of
+        // their own: scores are at most 2^15 * 2688 * D before sc, so a warp
+        // without such a row knows it here (in one loop the chunk is 2 % slower).
+        ok = __any_sync(0xffffffffu, sc * (88080384.0f * D) >= kFar) ? tiles(std::true_type{}) : tiles(std::false_type{});
       }
       tile_no += w.count;
       // ---- the unit's result, or this part's share of it.  A warp's rows are
