@@ -56,10 +56,10 @@
 //     ALU pipe 56 % busy (half of that are the E2M1 conversions, 2 cycles an
 //     instruction).  The copies alone, the arithmetic left out, run at 92 %.
 //     (5 query heads to each key/value head, as 8 rows.)
-//   32 sequences of 1 to 8,190 tokens (38 MB): 19 us; 1 of 512: 7.5 us, of
+//   32 sequences of 1 to 8,190 tokens (38 MB): 19 us; 1 of 512: 7.7 us, of
 //     which the launch, the plan, the first record's way from HBM and the join
 //     are 5: latency, not a rate.
-//   32 rows (16 sequences of 16,384, 4 query tokens by 8 heads): 136 us.  The
+//   32 rows (16 sequences of 16,384, 4 query tokens by 8 heads): 137 us.  The
 //     accumulators are 128 registers a thread, so two warps a scheduler run,
 //     and they wait for themselves (0.4 instructions a cycle).  Two 16-row
 //     tiles would convert everything twice.

@@ -38,9 +38,10 @@
 // Every wait is bounded.
 //
 // What bounds it (40 query heads on 8 key/value heads of 128).  A chunk of 2048
-// queries behind 16,385 tokens: 504 us, 1.45 PFLOP/s, 76 % of the measured bf16
-// burst rate and 85 % of the sustained one; nine sequences of 70 to 4,099 with
-// 1 to 701 queries: 83 us, 0.89 PFLOP/s.  A unit's beginning takes 6,000 cycles
+// queries behind 16,385 tokens: 501 us, 1.46 PFLOP/s, 76 % of the measured bf16
+// burst rate and 86 % of the sustained one (at head_dim 64, half the products:
+// 439 us); nine sequences of 70 to 4,099 with 1 to 701 queries: 84 us, 0.88
+// PFLOP/s.  A unit's beginning takes 6,000 cycles
 // (its queries' copies and conversion by 8 warps 4,500, the first scores 1,000)
 // and its end 4,500, during which the tensor pipe waits; starting the next
 // unit's queries under the last products gained nothing, for the same warps
@@ -49,7 +50,8 @@
 // loads and maxima 480, exponentials 1100, the P stores up to 640 while the
 // other tile's products use tensor memory), P V 600, and S again; two groups
 // alternate, so the tensor pipe works ~2400 of 3400 cycles a cached tile.  An
-// S ahead of P V needs 128 columns of TMEM more than there are.
+// S ahead of P V needs 128 columns of TMEM more than there are at head_dim 128
+// (at 64 they are free, and not used).
 // Tried and slower (the chunk, us, against 510): P announced in halves 569,
 // two threads a row 796, unpaired float arithmetic 523 to 547, the cached bytes
 // through a ring of bulk copies 610 (the operands' reads need the shared
@@ -71,7 +73,7 @@ constexpr int kSegSlots = 4;                 // segments announced ahead
 constexpr int kTile = 128;                   // cached tokens of a step; rows of a query tile
 constexpr int kRows = 2 * kTile;             // rows of a unit
 constexpr int kMinTiles = 4;                 // cached tiles worth a CTA
-constexpr int kUnitCost = 4;                 // what a unit's beginning and end cost, in tiles (nine mixed sequences: 3, 4, 5 give 87, 85, 85 us)
+constexpr int kUnitCost = 4;                 // what a unit's beginning and end cost, in tiles (11,000 cycles; a tile 3,400; 3 and 5 within 3 %)
 constexpr int kMaxBatch = 1024;
 constexpr float kShift = 14.0f, kSlack = 1.9f, kFar = 65536.0f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
